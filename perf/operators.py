@@ -358,8 +358,6 @@ def _handle(s):
     if "handle" not in s:
         import attention_score_kv_snapkv_gb300 as kvc
         s["handle"] = (kvc, kvc.KV8Cache.from_tensors(**s["cache"]))
-        s["tails"] = [s["cache"][n] for n in ("k_tail", "v_tail")]
-        s["tails0"] = [t.clone() for t in s["tails"]]
     return s["handle"]
 
 
@@ -375,8 +373,6 @@ def run(state):
     if c["op"] == "write":
         kvc.kv8_write(s["k"], s["v"], handle, lengths=s["lengths"])
     elif c["op"] == "append":
-        # the open block's rows come back too: the pass before left its own in the tail
-        torch._foreach_copy_(s["tails"], s["tails0"])
         kvc.kv8_append(s["k"], s["v"], handle, new_pos=c["filled"])
     elif c["op"] == "read":
         k, v = kvc.kv8_read(handle, k_out=s["k_out"], v_out=s["v_out"])
