@@ -67,7 +67,8 @@ class KV8Params(ctypes.Structure):
 class KV8CacheC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail", "pos", "n_valid",
-        "scratch")] + [("scratch_bytes", ctypes.c_size_t)]
+        "scratch")] + [("scratch_bytes", ctypes.c_size_t)] + [(n, ctypes.c_void_p) for n in (
+            "k_last", "v_last", "blocks")]
 
 
 _P = ctypes.c_void_p
@@ -622,10 +623,17 @@ class KV8Cache:
     [..,64,D] bf16 (the rows past the last whole block), pos [..,cap] int32 (may be None),
     n_valid [Ly,B,Hkv] int32 and the decode step's scratch.  cap is a multiple of 64.  The
     tensors are fixed when the cache is made (change them in place); calls on one cache must be
-    ordered, calls on different caches are independent."""
+    ordered, calls on different caches are independent.
+
+    Rows are taken back (a draft's rejected tokens) by lowering n_valid: to any row of the tail's
+    block or of the block that was completed last, or to a multiple of 64; other counts set
+    DEV_BAD_STATE.  For that the cache also has k_last, v_last [..,65,D] bf16 (that block's rows
+    as they came, and the tail's first row) and blocks [..,2] int32 (the tail's block and that
+    block).  A caller who puts another state into the tensors fills blocks with -1."""
 
     __slots__ = ("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail", "pos", "n_valid",
-                 "scratch", "shape", "cap", "head_dim", "device", "_index", "_c", "_ref")
+                 "scratch", "k_last", "v_last", "blocks", "shape", "cap", "head_dim", "device",
+                 "_index", "_c", "_ref")
 
     def __init__(self, n_layers, batch, n_kv_heads, head_dim, cap, device="cuda"):
         if cap < 1 or cap % KV8_BLOCK:
@@ -641,16 +649,19 @@ class KV8Cache:
 
     @classmethod
     def from_tensors(cls, k_codes, v_codes, k_scale, v_scale, k_tail, v_tail, n_valid, pos=None,
-                     scratch=None):
+                     scratch=None, k_last=None, v_last=None, blocks=None):
         """A cache over tensors the caller holds (shapes as above; they are not copied).
         scratch: zero-filled uint8, 256-byte aligned, kv8_scratch_bytes() long, or None to
         allocate it; caches of the same layers x batch x KV heads may share one if their calls
-        are ordered, others may not."""
+        are ordered, others may not.  k_last, v_last and blocks (filled with -1 at first): all
+        three, or None to allocate them; two caches over the same tensors share them too."""
         self = cls.__new__(cls)
-        self._set(k_codes, v_codes, k_scale, v_scale, k_tail, v_tail, n_valid, pos, scratch)
+        self._set(k_codes, v_codes, k_scale, v_scale, k_tail, v_tail, n_valid, pos, scratch, k_last,
+                  v_last, blocks)
         return self
 
-    def _set(self, k_codes, v_codes, k_scale, v_scale, k_tail, v_tail, n_valid, pos, scratch):
+    def _set(self, k_codes, v_codes, k_scale, v_scale, k_tail, v_tail, n_valid, pos, scratch,
+             k_last=None, v_last=None, blocks=None):
         _need(k_codes, "k_codes", torch.float8_e4m3fn)
         if k_codes.dim() != 5:
             raise ValueError("k_codes must be [layers, batch, kv_heads, cap, head_dim], got %s"
@@ -675,13 +686,24 @@ class KV8Cache:
             _need(scratch, "scratch", torch.uint8)
             if scratch.numel() < need:
                 raise ValueError("scratch must hold %d bytes, got %d" % (need, scratch.numel()))
-        every = (k_codes, v_codes, k_scale, v_scale, k_tail, v_tail, n_valid, scratch)
+        if (k_last is None) != (blocks is None) or (v_last is None) != (blocks is None):
+            raise ValueError("k_last, v_last and blocks come together")
+        if blocks is None:
+            k_last = torch.zeros(u + (KV8_BLOCK + 1, D), dtype=torch.bfloat16, device=k_codes.device)
+            v_last = torch.zeros_like(k_last)
+            blocks = torch.full(u + (2,), -1, dtype=torch.int32, device=k_codes.device)
+        else:
+            _need(k_last, "k_last", torch.bfloat16, u + (KV8_BLOCK + 1, D))
+            _need(v_last, "v_last", torch.bfloat16, u + (KV8_BLOCK + 1, D))
+            _need(blocks, "blocks", torch.int32, u + (2,))
+        every = (k_codes, v_codes, k_scale, v_scale, k_tail, v_tail, n_valid, scratch, k_last,
+                 v_last, blocks)
         for t in every + (() if pos is None else (pos,)):
             if t.device != k_codes.device:
                 raise ValueError("the cache's tensors must be on one device")
         fix = object.__setattr__
         for name, t in zip(("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail",
-                            "n_valid", "scratch"), every):
+                            "n_valid", "scratch", "k_last", "v_last", "blocks"), every):
             fix(self, name, t)
         fix(self, "pos", pos)
         fix(self, "shape", u)
@@ -691,7 +713,8 @@ class KV8Cache:
         fix(self, "_index", k_codes.device.index)
         fix(self, "_c", KV8CacheC(*(t.data_ptr() for t in every[:6]),
                                   None if pos is None else pos.data_ptr(), n_valid.data_ptr(),
-                                  scratch.data_ptr(), scratch.numel()))
+                                  scratch.data_ptr(), scratch.numel(), k_last.data_ptr(),
+                                  v_last.data_ptr(), blocks.data_ptr()))
         fix(self, "_ref", ctypes.byref(self._c))
 
     def __setattr__(self, name, value):

@@ -9,6 +9,7 @@
 namespace kvc {
 
 constexpr int KB8 = KVC_KV8_BLOCK;  // rows of one scale
+constexpr int KL8 = KB8 + 1;        // rows of a unit in k_last and v_last
 
 // The cache as the kernels see it.
 struct Kv8 {
@@ -17,8 +18,26 @@ struct Kv8 {
   __nv_bfloat16 *kt, *vt;      // [U, KB8, D] the rows past the last whole block
   int32_t *pos;                // [U, cap] or null
   int32_t *n_valid;            // [U]
+  // What lets a row count be lowered into a block that has been quantised since (all null: it may
+  // not be): the rows of the block that was completed last, as they came, and behind them a copy
+  // of the tail's first row as the last call left it; and for each unit x the block that the
+  // tail's rows belong to, y the block held here (-1: none).
+  __nv_bfloat16 *kl, *vl;      // [U, KL8, D]
+  int2 *blocks;                // [U]
   int units, D, cap;
 };
+
+// Where the rows of the block that n rows leave open are: in the tail, in kl and vl, or nowhere
+// any more.  The latter two only if the tail's first row is still the one that the last call
+// left: a tail that the caller has put other rows into is taken as it is.
+enum : int { OPEN_TAIL = 0, OPEN_LAST = 1, OPEN_GONE = 2 };
+__device__ __forceinline__ int open_rows(int n, int2 blk) {
+  if (n % KB8 == 0 || blk.x <= n / KB8) return OPEN_TAIL;
+  return blk.y == n / KB8 ? OPEN_LAST : OPEN_GONE;
+}
+__device__ __forceinline__ bool same16(uint4 a, uint4 b) {
+  return ((a.x ^ b.x) | (a.y ^ b.y) | (a.z ^ b.z) | (a.w ^ b.w)) == 0;
+}
 
 struct Kv8WriteArgs {
   Kv8 c;

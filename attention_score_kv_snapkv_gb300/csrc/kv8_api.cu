@@ -27,8 +27,10 @@ kvc_status check_cache(const kvc_kv8_params *p, const kvc_kv8_cache *x, Kv8 *c) 
   if (!x->k_codes || !x->v_codes || !x->k_scale || !x->v_scale || !x->k_tail || !x->v_tail || !x->n_valid)
     return KVC_ERR_NULL;
   if (!al(x->k_codes, 16) || !al(x->v_codes, 16) || !al(x->k_tail, 16) || !al(x->v_tail, 16) ||
-      !al(x->k_scale, 16) || !al(x->v_scale, 16) || !al(x->n_valid, 4) || !al(x->pos, 4))
+      !al(x->k_scale, 16) || !al(x->v_scale, 16) || !al(x->n_valid, 4) || !al(x->pos, 4) ||
+      !al(x->k_last, 16) || !al(x->v_last, 16) || !al(x->blocks, 8))
     return KVC_ERR_ALIGN;
+  if (!x->k_last != !x->blocks || !x->v_last != !x->blocks) return KVC_ERR_NULL;  // all or none
   c->kq = static_cast<uint8_t *>(x->k_codes);
   c->vq = static_cast<uint8_t *>(x->v_codes);
   c->ks = x->k_scale;
@@ -37,6 +39,9 @@ kvc_status check_cache(const kvc_kv8_params *p, const kvc_kv8_cache *x, Kv8 *c) 
   c->vt = static_cast<__nv_bfloat16 *>(x->v_tail);
   c->pos = x->pos;
   c->n_valid = x->n_valid;
+  c->kl = static_cast<__nv_bfloat16 *>(x->k_last);
+  c->vl = static_cast<__nv_bfloat16 *>(x->v_last);
+  c->blocks = reinterpret_cast<int2 *>(x->blocks);
   c->units = (int)units;
   c->D = p->head_dim;
   c->cap = p->cap;

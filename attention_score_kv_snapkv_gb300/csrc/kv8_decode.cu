@@ -32,7 +32,8 @@
 //   the whole CTA at its end.
 // * With an append every CTA reads the row counts before any changes: the last CTA to have
 //   planned (an atomic count) advances them, while the others already stream.  The CTA that
-//   has a unit's tail writes the new row, or quantises the block that it completes.
+//   has a unit's tail writes the new row, or quantises the block that it completes and keeps that
+//   block's rows as they came; a row count lowered into that block has the tail's tile from there.
 // * Every wait is bounded; one that runs out sets the device's timeout flag and the CTA drains.
 //
 // Warps: TMA; S; PV; queries; 2 x 4 softmax (alternate tiles); 4 output; merge.  Four tiles may
@@ -84,7 +85,7 @@ struct Geo {
   static constexpr int OFF_MT = OFF_MX + 2 * 2 * 8 * 4 * 4;  // float [NB][8] tile references
   static constexpr int OFF_ST = OFF_MT + NB * 8 * 4;        // float2 [2][8 warps][8] (max, normaliser)
   static constexpr int OFF_BAR = OFF_ST + 2 * 8 * 8 * 8 + 8 * 16;  // and float4 [8]
-  static constexpr int SMEM = OFF_BAR + 704 + 1024;
+  static constexpr int SMEM = OFF_BAR + 768 + 1024;
   static_assert(OFF_Q8 % 1024 == 0 && OFF_QT % 1024 == 0 && OFF_P % 1024 == 0, "operand alignment");
   static_assert(NST % 2 == 0 && SMEM <= 232448, "shared memory");
 };
@@ -110,7 +111,8 @@ constexpr int M_RED = 46;      // [4] quantisation
 constexpr int M_VALID = 50;    // [2] a shared unit's segment was completed
 constexpr int M_TODO = 52;     // [2][4] this CTA merges it at the end: the Shared (nseg 0: it does not)
 static_assert(sizeof(WaitState) == 4 * (M_TMEM - M_WAIT) && B_MISC % 8 == 0, "the waits' state");
-static_assert(B_MISC + 4 * (M_TODO + 8) <= 704, "barrier area");
+constexpr int M_RE = 60;       // [1 + SNAP / 32] whether, and which of, the CTA's units have their open rows in kl and vl
+static_assert(B_MISC + 4 * (M_RE + 1 + SNAP / 32) <= 768, "barrier area");
 
 struct P8 {
   const __nv_bfloat16 *q, *k_new, *v_new;
@@ -120,7 +122,7 @@ struct P8 {
   int ga, new_pos;
   int *planned;            // CTAs that have read the row counts
   int *cnt;                // [U] finished segments of a shared unit
-  int *snap;               // [U] row counts before the append
+  int *snap;               // [U] row counts before the append, negative (~n) with open rows in kl and vl
   float2 *part_ml;         // [2 * MAXCTA][G]
   float *part_o;           // [2 * MAXCTA][G][D]
   uint32_t *status;
@@ -287,9 +289,10 @@ struct Seg {
   int ntiles;
 };
 
-// The maps of K's and V's codes, in boxes of a tile and of a block, and of their tails.
+// The maps of K's and V's codes, in boxes of a tile and of a block, of their tails, and of the rows
+// of the block completed last.
 struct Maps {
-  CUtensorMap k, v, k1, v1, kt, vt;
+  CUtensorMap k, v, k1, v1, kt, vt, kl, vl;
 };
 
 // One shared unit: its segments' results are at part(0), part(1), ...
@@ -304,6 +307,72 @@ __device__ __forceinline__ float seg_weight(float2 ml, float m) {
 __device__ __forceinline__ uint2 bf4(float4 o, float inv) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
   return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
+// The CTA's i-th unit u has n rows, whose open ones are not where a tail's rows are: marked if they
+// are in kl and vl, reported if they are gone.  Out of line: a row count is rarely lowered.  (Another
+// CTA that has planned may already have written to the unit's tail; only the CTA that has the tail
+// goes by the mark.)
+template <int D>
+__device__ __noinline__ int reopened(const Kv8 &c, int u, int n, int open, uint32_t *status, int *marks, int i) {
+  constexpr int RV = D / 8;
+  bool left = true;  // the tail's first row is the one that the last call left
+#pragma unroll 1
+  for (int i = 0; i < 2 * RV; ++i) {
+    const uint4 *tl = reinterpret_cast<const uint4 *>(i < RV ? c.kt : c.vt) + (size_t)u * KB8 * RV;
+    const uint4 *ls = reinterpret_cast<const uint4 *>(i < RV ? c.kl : c.vl) + ((size_t)u * KL8 + KB8) * RV;
+    left &= same16(__ldcg(tl + i % RV), __ldcg(ls + i % RV));
+  }
+  if (left && open == OPEN_GONE) set_status(status, KVC_DEV_BAD_STATE);
+  if (!left || open != OPEN_LAST) return n;
+  marks[0] = 1;
+  if (i >= SNAP) return ~n;
+  atomicOr(marks + 1 + i / 32, 1 << (i % 32));
+  return n;
+}
+
+// The new row is the first of a block, or joins rows that are kept: the kept ones go back to the tail,
+// unless the block is then complete.  By a warp.  (What is written here concerns the unit's open rows,
+// so it misleads no CTA but the one that has them, which has planned.)
+template <int D>
+__device__ __noinline__ void open_block(const P8 &p, int u, int n0, int lane) {
+  constexpr int RV = D / 8;
+  const int r = n0 % KB8;
+  if (r == KB8 - 1) return;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint4 *tail = reinterpret_cast<uint4 *>(h ? p.c.vt : p.c.kt) + (size_t)u * KB8 * RV;
+    uint4 *kept = reinterpret_cast<uint4 *>(h ? p.c.vl : p.c.kl) + (size_t)u * KL8 * RV;
+#pragma unroll 8
+    for (int e = lane; e < r * RV; e += 32) tail[e] = __ldcg(kept + e);
+    const uint4 *first = r > 0 ? kept : reinterpret_cast<const uint4 *>(h ? p.v_new : p.k_new) + (size_t)u * RV;
+    if (lane < RV) kept[KB8 * RV + lane] = __ldcg(first + lane);
+  }
+  if (lane == 0 && (r > 0 || p.c.blocks[u].x != n0 / KB8)) p.c.blocks[u] = make_int2(n0 / KB8, -1);
+}
+
+// Quantises unit u's block nb, which the new row completes, and keeps its rows as they came, by the
+// 128 output threads; re: the other rows are the kept ones.
+template <int D>
+__device__ __noinline__ void complete(const P8 &p, int u, int nb, bool re, uint32_t *red, int t) {
+  constexpr int RV = D / 8, NP = KB8 * RV / KV8_NT, RS = KV8_NT / RV;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    const uint4 *xn = reinterpret_cast<const uint4 *>(h ? p.v_new : p.k_new) + (size_t)u * RV;
+    uint4 *kept = reinterpret_cast<uint4 *>(h ? p.c.vl : p.c.kl) + (size_t)u * KL8 * RV;
+    const uint4 *old = re ? kept : reinterpret_cast<const uint4 *>(h ? p.c.vt : p.c.kt) + (size_t)u * KB8 * RV;
+    uint4 w[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) w[i] = t / RV + i * RS < KB8 - 1 ? old[t + i * KV8_NT] : xn[t % RV];
+    if (p.c.blocks) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) kept[t + i * KV8_NT] = w[i];
+      if (!re && t < RV) kept[KB8 * RV + t] = w[0];  // the tail's first row is this block's
+      if (h == 0 && t == 0) p.c.blocks[u] = make_int2(nb + 1, nb);
+    }
+    quantise_block<D>(w, (h ? p.c.vq : p.c.kq) + ((size_t)u * p.c.cap + (size_t)nb * KB8) * D,
+                      (h ? p.c.vs : p.c.ks) + (size_t)u * (p.c.cap / KB8) + nb, red, 3, t);
+  }
 }
 
 // Merges a shared unit's few segments (at most FEW) by nt threads, t of them this one.
@@ -387,7 +456,7 @@ __device__ __forceinline__ void merge_cta(const P8 &p, const Shared &x, float *b
 
 template <int D, int G>
 __global__ void __launch_bounds__(NTH, 1)
-    kv8_decode_kernel(const __grid_constant__ Maps maps, const P8 p) {
+    kv8_decode_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P8 p) {
   using Gm = Geo<D, G>;
   constexpr int HB = Gm::HB, KPR = Gm::KPR, TB = Gm::TB, PN = Gm::PN, NST = Gm::NST;
   using Stage = StageOf<NST>;
@@ -435,6 +504,7 @@ __global__ void __launch_bounds__(NTH, 1)
     tma_prefetch_desc(&maps.kt);
     tma_prefetch_desc(&maps.vt);
   }
+  if (warp == W_M && lane <= SNAP / 32) misc[M_RE + lane] = 0;
   if (warp == W_S) {
     tmem_alloc(smem_u32(const_cast<int *>(misc + M_TMEM)), TMEM_COLS);
     tmem_relinquish();
@@ -447,12 +517,15 @@ __global__ void __launch_bounds__(NTH, 1)
   const int per = (U + NTH - 1) / NTH;
   const int ua = min(U, tid * per), ub = min(U, ua + per);
   int sum = 0, n_own = 0;  // n_own: the row count of this thread's unit where it has only one
+  int open_own = OPEN_TAIL;  // and where that one's open rows are
   constexpr int TW = TB * (HB / 4);  // slots of a tail and a unit's end: about a tile's time, two with 8 heads
   uint32_t odd = 0;
 #pragma unroll 4
   for (int u = ua; u < ub; ++u) {
     const int n = p.c.n_valid[u];
+    const int2 blk = per == 1 && p.c.blocks ? p.c.blocks[u] : make_int2(-1, -1);
     n_own = clamped(n);
+    open_own = open_rows(n_own, blk);
     sum += n_own / KB8 + TW;
     odd |= n != n_own ? KVC_DEV_BAD_STATE : (app && n == cap ? KVC_DEV_CACHE_FULL : 0u);
   }
@@ -528,14 +601,17 @@ __global__ void __launch_bounds__(NTH, 1)
   const int u_first = uniform(misc[M_UF]), p_first = uniform(misc[M_PF]), u_last = uniform(misc[M_UL]),
             p_last = uniform(misc[M_PL]);
   const int nu = s0 < s1 ? max(u_last - u_first + 1, 0) : 0;
-  if (per == 1) {
-    if (ua < ub && ua >= u_first && ua - u_first < nu) sn[ua - u_first] = n_own;
-  } else {
-    for (int i = tid; i < nu; i += NTH) {
-      const int n = clamped(p.c.n_valid[u_first + i]);
-      if (i < SNAP) sn[i] = n;
-      else p.snap[u_first + i] = n;  // a neighbour that shares the unit writes the same
+#pragma unroll 1
+  for (int i = per > 1 ? tid : (ua < ub && ua >= u_first ? ua - u_first : nu); i < nu; i += NTH) {
+    const int u = u_first + i;
+    int n = n_own, open = open_own;
+    if (per > 1) {
+      n = clamped(p.c.n_valid[u]);
+      open = p.c.blocks ? open_rows(n, p.c.blocks[u]) : OPEN_TAIL;
     }
+    if (open != OPEN_TAIL) n = reopened<D>(p.c, u, n, open, p.status, const_cast<int *>(misc + M_RE), i);
+    if (i < SNAP) sn[i] = n;
+    else p.snap[u] = n;
   }
   __syncthreads();
   // The slots at which its first unit's share begins and its last one's ends, within the unit.  (By
@@ -547,7 +623,7 @@ __global__ void __launch_bounds__(NTH, 1)
     const int i = k == 0 ? nu - 1 : k - 1;
     Seg g;
     g.u = u_first + i;
-    g.n0 = i < SNAP ? sn[i] : p.snap[g.u];
+    g.n0 = i < SNAP ? sn[i] : max(p.snap[g.u], ~p.snap[g.u]);
     g.add = app && g.n0 < cap;
     const int nb = g.n0 / KB8;
     g.lo = i == 0 ? lo_first : 0;
@@ -560,6 +636,12 @@ __global__ void __launch_bounds__(NTH, 1)
     g.nt = g.tail ? g.tail_old + (g.add ? 1 : 0) : 0;
     g.ntiles = g.t8 + (g.nt > 0 ? 1 : 0);
     return g;
+  };
+  // Whether unit u's open rows are in kl and vl.
+  auto kept_rows = [&](int u) {
+    if (misc[M_RE] == 0) return false;
+    const int i = u - u_first;
+    return i < SNAP ? ((misc[M_RE + 1 + i / 32] >> (i % 32)) & 1) != 0 : p.snap[u] < 0;
   };
   auto shared_at = [&](const Seg &g) {
     Shared x;
@@ -607,6 +689,8 @@ __global__ void __launch_bounds__(NTH, 1)
           // when the first unit's have come.
           if (tiles == 1 && !wait.all(bar + B_START, 0)) { ok = false; break; }
           const int nblk = min(TB, g.b_hi - g.lo - TB * i), boxes = (g.tail_old + 15) / 16;
+          const bool kept = i >= g.t8 && kept_rows(g.u);
+          const int open_row = g.u * (kept ? KL8 : KB8);
           auto load = [&](Stage &x, const CUtensorMap *whole, const CUtensorMap *one, const CUtensorMap *tail) {
             if (!wait.all(bar + B_EMPTY + 8 * x.st, x.ph ^ 1)) return false;
             const uint32_t dst = sb + x.st * SB, full = bar + B_FULL + 8 * x.st;
@@ -624,12 +708,16 @@ __global__ void __launch_bounds__(NTH, 1)
               for (int kb = 0; kb < Gm::KBT; ++kb)
 #pragma unroll 1
                 for (int j = 0; j < boxes; ++j)
-                  tma_load(lead, dst + kb * KB8 * 128 + j * 2048, tail, kb * 64, g.u * KB8 + j * 16, full);
+                  tma_load(lead, dst + kb * KB8 * 128 + j * 2048, tail, kb * 64, open_row + j * 16, full);
             }
             x.next();
             return true;
           };
-          if (!load(k8, &maps.k, &maps.k1, &maps.kt) || !load(v8, &maps.v, &maps.v1, &maps.vt)) { ok = false; break; }
+          if (!load(k8, &maps.k, &maps.k1, kept ? &maps.kl : &maps.kt) ||
+              !load(v8, &maps.v, &maps.v1, kept ? &maps.vl : &maps.vt)) {
+            ok = false;
+            break;
+          }
         }
       }
       // drain: every load issued has arrived before the CTA may exit (the last use of each stage)
@@ -1165,27 +1253,20 @@ __global__ void __launch_bounds__(NTH, 1)
         asm volatile("bar.arrive %0, 160;" ::"r"(4 + si) : "memory");  // W_M counts it
         ++si;
       }
-      if (g.tail && g.add && g.tail_old == KB8 - 1) {  // the new row completes a block
-        constexpr int RV = D / 8, NP = KB8 * RV / KV8_NT, RS = KV8_NT / RV;
-        const int nb = g.n0 / KB8;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          const uint4 *xn = reinterpret_cast<const uint4 *>(h ? p.v_new : p.k_new) + (size_t)g.u * RV;
-          const uint4 *tl = reinterpret_cast<const uint4 *>(h ? p.c.vt : p.c.kt) + (size_t)g.u * KB8 * RV;
-          uint4 w[NP];
-#pragma unroll
-          for (int i = 0; i < NP; ++i) w[i] = te / RV + i * RS < KB8 - 1 ? tl[te + i * KV8_NT] : xn[te % RV];
-          quantise_block<D>(w, (h ? p.c.vq : p.c.kq) + ((size_t)g.u * cap + (size_t)nb * KB8) * D,
-                            (h ? p.c.vs : p.c.ks) + (size_t)g.u * (cap / KB8) + nb,
-                            reinterpret_cast<uint32_t *>(const_cast<int *>(misc + M_RED)), 3, te);
-        }
-      }
+      if (g.tail && g.add && g.tail_old == KB8 - 1)  // the new row completes a block
+        complete<D>(p, g.u, g.n0 / KB8, kept_rows(g.u), reinterpret_cast<uint32_t *>(const_cast<int *>(misc + M_RED)), te);
     }
   } else {
     // ---------------- shared units ----------------
     // The CTA that finishes a shared unit's last segment merges them: this warp, while the
     // others stream on (a fence and a count take microseconds behind the tiles), or the whole
     // CTA at its end.  Only the first two segments of a CTA can be of shared units.
+    if (app && p.c.blocks)
+#pragma unroll 1
+      for (int k = 0; k < nu; ++k) {
+        const Seg g = seg_at(k);
+        if (g.tail && g.add && (g.tail_old == 0 || kept_rows(g.u))) open_block<D>(p, g.u, g.n0, lane);
+      }
     int si = 0;
     auto count_shared = [&](int k) {
       const Seg g = seg_at(k);
@@ -1245,6 +1326,10 @@ cudaError_t launch_t(const Ctx &c, const Kv8DecodeArgs &a, const P8 &p) {
   if (!encode_bytes_map(&m.k, a.c.kq, rows, TROWS) || !encode_bytes_map(&m.v, a.c.vq, rows, TROWS) ||
       !encode_bytes_map(&m.k1, a.c.kq, rows, Gm::BR) || !encode_bytes_map(&m.v1, a.c.vq, rows, Gm::BR) ||
       !encode_rows_map(&m.kt, a.c.kt, trows, D, 16) || !encode_rows_map(&m.vt, a.c.vt, trows, D, 16))
+    return cudaErrorInvalidValue;
+  m.kl = m.kt, m.vl = m.vt;  // not used without kept rows
+  const uint64_t lrows = (uint64_t)a.c.units * KL8;
+  if (a.c.blocks && (!encode_rows_map(&m.kl, a.c.kl, lrows, D, 16) || !encode_rows_map(&m.vl, a.c.vl, lrows, D, 16)))
     return cudaErrorInvalidValue;
   const long long slots = (long long)a.c.units * (a.c.cap / KB8 + 1);
   long long grid = c.num_sms < MAXCTA ? c.num_sms : MAXCTA;

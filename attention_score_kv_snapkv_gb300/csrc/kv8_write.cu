@@ -32,6 +32,14 @@ cudaError_t launch_overlapped(cudaStream_t stream, unsigned grid, void (*kernel)
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The kept copy of the tail's first row, and the rows of the block completed last before it.
+__device__ __forceinline__ uint4 *last_rows(const Kv8 &c, int u, bool is_v) {
+  return reinterpret_cast<uint4 *>(is_v ? c.vl : c.kl) + (size_t)u * KL8 * (c.D / 8);
+}
+__device__ __forceinline__ uint4 *first_row(const Kv8 &c, int u, bool is_v) {
+  return last_rows(c, u, is_v) + KB8 * (c.D / 8);
+}
+
 // Grid: units x blocks x {K, V}, K and V of a block next to each other; a CTA takes both where
 // rows are 64 wide (half as much each: as many bytes in flight, half as many CTAs).  Loads are
 // without branches, so that all of a thread's are in flight at once.
@@ -66,6 +74,7 @@ __global__ void __launch_bounds__(KV8_NT, 10) kv8_write_kernel(const Kv8WriteArg
             r >= n ? -1 : (a.pos_in ? a.pos_in[(size_t)u * a.n_rows + r] : (map ? map[r] : r));
     if (b == 0 && t == 0) a.c.n_valid[u] = n;
   }
+  if (a.c.blocks && first == 0 && b == 0 && t == 0) a.c.blocks[u] = make_int2(n / KB8, -1);
   if (b * KB8 >= n) return;
   const int piece = t % RV, row0 = t / RV;
   uint4 w[NX][NP];
@@ -89,11 +98,15 @@ __global__ void __launch_bounds__(KV8_NT, 10) kv8_write_kernel(const Kv8WriteArg
       uint8_t *dst = (is_v ? a.c.vq : a.c.kq) + ((size_t)u * a.c.cap + (size_t)b * KB8) * D;
       float *sc = (is_v ? a.c.vs : a.c.ks) + (size_t)u * (a.c.cap / KB8) + b;
       quantise_block<D>(w[x], dst, sc, red, 1, t);
+      if (a.c.blocks && (b + 1) * KB8 == n && t < RV)  // no open rows: the tail stays as it was
+        first_row(a.c, u, is_v)[t] = __ldcg(reinterpret_cast<const uint4 *>(is_v ? a.c.vt : a.c.kt) +
+                                            (size_t)u * KB8 * RV + t);
     } else {
       uint4 *tail = reinterpret_cast<uint4 *>(is_v ? a.c.vt : a.c.kt) + (size_t)u * KB8 * RV;
 #pragma unroll
       for (int i = 0; i < NP; ++i)
         if (b * KB8 + row0 + i * RS < n) tail[t + i * KV8_NT] = w[x][i];
+      if (a.c.blocks && t < RV) first_row(a.c, u, is_v)[t] = w[x][0];
     }
   }
 }
@@ -101,6 +114,8 @@ __global__ void __launch_bounds__(KV8_NT, 10) kv8_write_kernel(const Kv8WriteArg
 // Adds rows to every unit.  Grid: units x {K, V} x CTAs; CTA j takes the j-th block that fills,
 // and CTA 0, whose block starts with the tail's rows, then writes the new tail.  The row count
 // changes when every CTA of the unit has read it: the last one to count itself writes it.
+// The rows of one completed block are kept as they came, so that the row count may be lowered into
+// it: the block that held rows before, else the last one (64 units of 700 rows: 64 KB more to 358).
 template <int D>
 __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8AppendArgs a, int per, uint32_t *status) {
   constexpr int RV = D / 8, NP = KB8 * RV / KV8_NT, RS = KV8_NT / RV;
@@ -121,12 +136,24 @@ __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8AppendArgs 
   uint4 *tail = reinterpret_cast<uint4 *>(is_v ? a.c.vt : a.c.kt) + (size_t)u * KB8 * RV;
   const int piece = t % RV, row0 = t / RV;
   const bool fills = b < last;
-  uint4 w[NP];
+  const int2 blk = a.c.blocks ? a.c.blocks[u] : make_int2(-1, -1);
+  const int keep = n0 % KB8 ? n0 / KB8 : last - 1;        // the completed block whose rows are kept
+  const bool opens = a.c.blocks && j == 0 && m > 0;       // this CTA leaves the tail's first row
+  uint4 w[NP], head = make_uint4(0, 0, 0, 0);             // head: the tail's first row
+  const uint4 *old = tail;                                // the open block's rows
+  if (opens) {
+    if (t < RV) head = tail[t];
+    const int open = open_rows(n0, blk);
+    if (open != OPEN_TAIL && __syncthreads_and(t >= RV || same16(head, first_row(a.c, u, is_v)[t]))) {
+      if (open == OPEN_LAST) old = last_rows(a.c, u, is_v);
+      else if (t == 0) set_status(status, KVC_DEV_BAD_STATE);
+    }
+  }
   if (fills) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int r = b * KB8 + row0 + i * RS;
-      w[i] = r < n0 ? tail[t + i * KV8_NT] : __ldg(src + (size_t)(r - n0) * RV + piece);
+      w[i] = r < n0 ? old[t + i * KV8_NT] : __ldg(src + (size_t)(r - n0) * RV + piece);
     }
   }
   __syncthreads();  // every thread has read the row count, and the tail if it is to be read
@@ -135,23 +162,32 @@ __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8AppendArgs 
     if (atomicAdd(a.cnt + u, 1) == 2 * per - 1) {
       a.cnt[u] = 0;
       a.c.n_valid[u] = n1;
+      if (a.c.blocks && m > 0)
+        a.c.blocks[u] = make_int2(last, last > n0 / KB8 ? keep : (blk.x == n0 / KB8 ? blk.y : -1));
     }
   }
   if (fills) {
+    if (a.c.blocks && b == keep) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) last_rows(a.c, u, is_v)[t + i * KV8_NT] = w[i];
+    }
     uint8_t *dst = (is_v ? a.c.vq : a.c.kq) + ((size_t)u * a.c.cap + (size_t)b * KB8) * D;
     quantise_block<D>(w, dst, (is_v ? a.c.vs : a.c.ks) + (size_t)u * (a.c.cap / KB8) + b, red, 1, t);
   }
   if (j == 0) {  // the open block's new rows; rows of the tail behind them stay as they were
+    const int from = old != tail && !fills ? last * KB8 : n0;  // rows that are not in the tail yet
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int r = last * KB8 + row0 + i * RS;
-      w[i] = r >= n0 && r < n1 ? __ldg(src + (size_t)(r - n0) * RV + piece) : make_uint4(0, 0, 0, 0);
+      w[i] = r >= n0 && r < n1 ? __ldg(src + (size_t)(r - n0) * RV + piece)
+                               : (r >= from && r < n0 ? old[t + i * KV8_NT] : make_uint4(0, 0, 0, 0));
     }
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int r = last * KB8 + row0 + i * RS;
-      if (r >= n0 && r < n1) tail[t + i * KV8_NT] = w[i];
+      if (r >= from && r < n1) tail[t + i * KV8_NT] = w[i];
     }
+    if (opens && t < RV) first_row(a.c, u, is_v)[t] = last * KB8 >= from && last * KB8 < n1 ? w[0] : head;
   }
   if (!is_v && a.c.pos)
     for (int r = n0 + j * KV8_NT + t; r < n1; r += per * KV8_NT)
@@ -172,6 +208,14 @@ __global__ void __launch_bounds__(KV8_NT) kv8_read_kernel(const Kv8ReadArgs a, i
   const int whole = n / KB8;
   const int lim = min(n, a.out_rows);
   if (b * KB8 >= lim) return;
+  const uint4 *tail = reinterpret_cast<const uint4 *>(is_v ? a.c.vt : a.c.kt) + (size_t)u * KB8 * RV;
+  if (b == whole && a.c.blocks) {
+    const int open = open_rows(n, a.c.blocks[u]);
+    if (open != OPEN_TAIL && __syncthreads_and(t >= RV || same16(tail[t], first_row(a.c, u, is_v)[t]))) {
+      if (open == OPEN_LAST) tail = last_rows(a.c, u, is_v);
+      else if (t == 0) set_status(status, KVC_DEV_BAD_STATE);
+    }
+  }
   const int row0 = t / RV;
   uint4 *dst = reinterpret_cast<uint4 *>(is_v ? a.v : a.k) + ((size_t)u * a.out_rows + (size_t)b * KB8) * RV;
   if (b < whole) {
@@ -194,10 +238,9 @@ __global__ void __launch_bounds__(KV8_NT) kv8_read_kernel(const Kv8ReadArgs a, i
       if (b * KB8 + row0 + i * RS < lim) dst[t + i * KV8_NT] = o;
     }
   } else {
-    const uint4 *src = reinterpret_cast<const uint4 *>(is_v ? a.c.vt : a.c.kt) + (size_t)u * KB8 * RV;
 #pragma unroll
     for (int i = 0; i < NP; ++i)
-      if (b * KB8 + row0 + i * RS < lim) dst[t + i * KV8_NT] = src[t + i * KV8_NT];
+      if (b * KB8 + row0 + i * RS < lim) dst[t + i * KV8_NT] = tail[t + i * KV8_NT];
   }
 }
 

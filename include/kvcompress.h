@@ -393,6 +393,18 @@ typedef struct {
  * finite.  An infinity or a NaN is held as NaN.  A block is quantised once, when its last
  * row arrives: what the cache holds does not depend on how many calls brought its rows.
  * Rows of codes, scales and tail that hold none of the n rows are left as they were.
+ *
+ * Rows are taken back by lowering n_valid (on the device, between calls): to any row of the
+ * block whose rows the tail holds, or to a multiple of KVC_KV8_BLOCK; and where the cache has
+ * k_last, v_last and blocks, to any row of the block that was completed last (of a call that
+ * completed several: the one that held rows before the call, else the last).  The rows that
+ * remain are held as if the others had never been there; until rows are added again, n_valid
+ * may also be put back.  The bf16 rows of any other block are gone: a row count inside one sets
+ * KVC_DEV_BAD_STATE in the calls that need them (it is not noticed without k_last, v_last and
+ * blocks, nor of blocks completed before blocks was first used).  A tail whose first row is not
+ * the one that the last call left is taken as rows of the caller's own; a caller who puts another
+ * state into the buffers fills blocks with -1.
+ *
  * A call's other arguments may not overlap the cache's buffers, and its outputs nothing else
  * but where said. */
 typedef struct {       /* all dev pointers, owned by the caller; codes, scales and tails
@@ -410,6 +422,12 @@ typedef struct {       /* all dev pointers, owned by the caller; codes, scales a
                           Caches of the same number of units U may share one if their calls
                           are ordered; caches of different U may not */
   size_t scratch_bytes;
+  void *k_last;        /* bf16 [U, KVC_KV8_BLOCK + 1, D], 16-byte aligned: the rows of the
+                          block completed last, as they came, and the tail's first row */
+  void *v_last;        /* the same of V */
+  int32_t *blocks;     /* int32 [U, 2], 8-byte aligned, filled with -1 at first: the block of
+                          the tail's rows, and the block in k_last and v_last.  All three, or
+                          NULL: then n_valid is not lowered into a completed block */
 } kvc_kv8_cache;
 
 /* Bytes of scratch kv8_append and kv8_decode_attn need for p->n_q_heads (more query heads
