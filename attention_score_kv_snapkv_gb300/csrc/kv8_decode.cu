@@ -12,7 +12,8 @@
 // * O^T = V^T . P^T (128 lanes x 16 or 32 columns): a weight is split the same way into three
 //   e4m3 terms (12 bits), a column each.  The weight of key j in a tile is
 //   exp2(s_j + log2 scale_v - M) with M the tile's largest s_j + log2 scale_v, so V's scale
-//   costs nothing and blocks of very different sizes lose no bits to each other.  A tile's
+//   costs nothing and blocks of very different sizes lose no bits to each other.  (A block of zeros
+//   has the scale 1, which says nothing of its size: it is looked for, and counts with the least.)  A tile's
 //   product is not accumulated in tensor memory: four warps read it, one lane a thread, and add
 //   it to their registers with the running maximum's factor, so nothing in tensor memory is
 //   ever rescaled, and a weight keeps 12 bits down to 2^-14 of its own tile's largest and is
@@ -253,6 +254,31 @@ __device__ __forceinline__ __half2 half_e4m3x2(uint32_t codes) {
   return *reinterpret_cast<const __half2 *>(&h);
 }
 __device__ __forceinline__ float fin(float m) { return m == -INFINITY ? 0.f : m; }
+// vs: the V scales of a warp's tiles, one a lane, whose 4096 bytes of codes (of block blk) are at rows +
+// blk * block_bytes.  A block of zeros has the scale 1, which says nothing of its size, and would let
+// its keys set the reference of a tile whose other blocks are small: where the codes are zeros (and
+// NaNs, which come out whatever their weight is) alone, the scale becomes the least there is.  Looked at
+// only where a scale is 1, and a block that is not zeros mostly shows it in its first 16 codes.
+__device__ __forceinline__ bool zero_codes(const uint4 *at) {
+  const uint4 x = __ldcg(at);
+  // a magnitude m that is neither 0 nor 127 leaves a bit of m + 1 between the lowest and the highest
+  return ((((x.x & 0x7f7f7f7fu) + 0x01010101u) | ((x.y & 0x7f7f7f7fu) + 0x01010101u) |
+           ((x.z & 0x7f7f7f7fu) + 0x01010101u) | ((x.w & 0x7f7f7f7fu) + 0x01010101u)) & 0x7e7e7e7eu) == 0;
+}
+__device__ __noinline__ float without_zeros(const uint8_t *rows, int block_bytes, int blk, float vs, int lane) {
+  const uint8_t *mine = rows + (size_t)blk * block_bytes;
+  uint32_t todo = __ballot_sync(0xffffffffu, vs == 1.f && zero_codes(reinterpret_cast<const uint4 *>(mine)));
+#pragma unroll 1
+  for (; todo != 0; todo &= todo - 1) {
+    const int src = __ffs(todo) - 1;
+    const uint4 *at = reinterpret_cast<const uint4 *>(rows + (size_t)__shfl_sync(0xffffffffu, blk, src) * block_bytes);
+    bool zero = true;
+#pragma unroll 2  // few registers: the softmax warps keep theirs over the call
+    for (int i = 0; i < 8; ++i) zero &= zero_codes(at + lane + 32 * i);
+    if (__all_sync(0xffffffffu, zero) && lane == src) vs = 0x1p-126f;
+  }
+  return vs;
+}
 // 2^(m - to), the factor of a sum kept relative to m (-inf: an empty one, or NaN, which stays)
 __device__ __forceinline__ float rescale(float m, float to) { return m == -INFINITY ? 0.f : ex2(m - to); }
 
@@ -960,7 +986,7 @@ __global__ void __launch_bounds__(NTH, 1)
       const bool in = i < g.t8 && blk < g.b_hi;
       const size_t at = (size_t)g.u * (cap / KB8) + blk;
       ks = in ? __ldg(p.c.ks + at) : 1.f;
-      vs = in ? __ldg(p.c.vs + at) : 1.f;
+      vs = in ? __ldg(p.c.vs + at) : 0.5f;  // not 1
     };
     int sc = 0, ka = 0;
     bool ok = true;  // after a wait ran out the warps still meet at every barrier
@@ -983,6 +1009,9 @@ __global__ void __launch_bounds__(NTH, 1)
         const bool tail = i >= g.t8;
         if ((own & 31) == 0) {
           if (own > 0) ksl = ksl2, vsl = vsl2;
+          if (__any_sync(0xffffffffu, vsl == 1.f))
+            vsl = without_zeros(p.c.vq + (size_t)g.u * cap * D + (D == 128 ? (quarter & 1) * 4096 : 0), KB8 * D,
+                                g.lo + TB * (first + 2 * (own + lane)) + bo, vsl, lane);
           if (g.t8 > 2 * (own + 32)) scales(g, first, own / 32 + 1, ksl2, vsl2);
         }
         const float ks = __shfl_sync(0xffffffffu, ksl, own & 31), vs = tail ? 1.f : __shfl_sync(0xffffffffu, vsl, own & 31);
