@@ -1197,6 +1197,9 @@ __global__ void __launch_bounds__(NTH, 1)
           if (quarter == 0) mbar_arrive(bar + B_EMPTY + 8 * v8.st);
         }
         const bool tail = i >= g.t8;
+        if (tail)  // a weight's second term may be zero or negative: an infinity of V times the first is what counts
+#pragma unroll
+          for (int h = 0; h < G; ++h) o[h] = fabsf(o[h]) == INFINITY ? o[h] : o[h] + o[HB + h];
         bool grew = false;
 #pragma unroll
         for (int h = 0; h < G; ++h) grew |= mtile[h] > M[h];
@@ -1210,7 +1213,7 @@ __global__ void __launch_bounds__(NTH, 1)
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           const float c = rescale(mtile[h], M[h]);
-          const float x = tail ? (d < D ? o[h] + o[HB + h] : 0.f)
+          const float x = tail ? (d < D ? o[h] : 0.f)
                                : fmaf(fmaf(o[2 * HB + h], 0.0625f, o[HB + h]), 0.0625f, o[h]) * 0x1p-8f;
           acc[h] += x * c;
         }

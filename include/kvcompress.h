@@ -466,7 +466,8 @@ kvc_status kv8_read(const kvc_kv8_params *p, const kvc_kv8_cache *cache, int32_t
  * KVC_DEV_CACHE_FULL), then for each query head out = softmax(q . K^T / sqrt(D)) . V over the
  * unit's n rows: the blocks that were whole before this call in 8 bits, the rest, the new
  * row among it, in bf16 (a block that the new row completes is quantised by this call, after
- * it was attended).  n = 0 gives zeros.  q, out: dev bf16 [Ly,B,Hq,D].  out may be q itself;
+ * it was attended).  A NaN held in V and an infinity of V in an open row come out in their
+ * column.  n = 0 gives zeros.  q, out: dev bf16 [Ly,B,Hq,D].  out may be q itself;
  * any other overlap with q, k_new or v_new is KVC_ERR_SHAPE.
  * Uses the cache's scratch; a call that returns normally leaves it ready for the next (after
  * KVC_DEV_TIMEOUT, zero it again).  Limits: G in 1..8 and U <= KVC_DECODE_MAX_UNITS.
