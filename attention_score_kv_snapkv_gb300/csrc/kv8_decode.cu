@@ -985,8 +985,9 @@ __global__ void __launch_bounds__(NTH, 1)
       const int i = first + 2 * (chunk * 32 + lane), blk = g.lo + TB * i + bo;
       const bool in = i < g.t8 && blk < g.b_hi;
       const size_t at = (size_t)g.u * (cap / KB8) + blk;
-      ks = in ? __ldg(p.c.ks + at) : 1.f;
-      vs = in ? __ldg(p.c.vs + at) : 0.5f;  // not 1
+      // (not by way of the read-only cache: the step before writes scales while this CTA may be resident)
+      ks = in ? __ldcg(p.c.ks + at) : 1.f;
+      vs = in ? __ldcg(p.c.vs + at) : 0.5f;  // not 1
     };
     int sc = 0, ka = 0;
     bool ok = true;  // after a wait ran out the warps still meet at every barrier

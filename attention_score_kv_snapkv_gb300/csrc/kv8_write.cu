@@ -16,7 +16,9 @@ namespace {
 // The write and the append may be launched while the kernel before them in the stream still runs,
 // and wait for it (an append of 700 rows 9.6 us against 10.3).  They let the next one be launched
 // only by ending: an early trigger made a selection every time 38.7 us instead of 34.7; and the
-// read-back, one short wave, took 3.8 us so and 2.8 launched plainly.
+// read-back, one short wave, took 3.8 us so and 2.8 launched plainly.  Their sources may have been
+// written by the kernel that they overlap, so they are not loaded by way of the read-only cache, whose
+// lines that kernel's end does not renew.
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename... P, typename... A>
 cudaError_t launch_overlapped(cudaStream_t stream, unsigned grid, void (*kernel)(P...), A... args) {
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(KV8_NT, 10) kv8_write_kernel(const Kv8WriteArg
 #pragma unroll
     for (int x = 0; x < NX; ++x) {
       const uint4 *src = reinterpret_cast<const uint4 *>(first + x ? a.v : a.k) + (size_t)u * a.L * RV;
-      w[x][i] = in ? __ldg(src + (size_t)s * RV + piece) : make_uint4(0, 0, 0, 0);
+      w[x][i] = in ? __ldcg(src + (size_t)s * RV + piece) : make_uint4(0, 0, 0, 0);
     }
   }
 #pragma unroll
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8AppendArgs 
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int r = b * KB8 + row0 + i * RS;
-      w[i] = r < n0 ? old[t + i * KV8_NT] : __ldg(src + (size_t)(r - n0) * RV + piece);
+      w[i] = r < n0 ? old[t + i * KV8_NT] : __ldcg(src + (size_t)(r - n0) * RV + piece);
     }
   }
   __syncthreads();  // every thread has read the row count, and the tail if it is to be read
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8AppendArgs 
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int r = last * KB8 + row0 + i * RS;
-      w[i] = r >= n0 && r < n1 ? __ldg(src + (size_t)(r - n0) * RV + piece)
+      w[i] = r >= n0 && r < n1 ? __ldcg(src + (size_t)(r - n0) * RV + piece)
                                : (r >= from && r < n0 ? old[t + i * KV8_NT] : make_uint4(0, 0, 0, 0));
     }
 #pragma unroll
