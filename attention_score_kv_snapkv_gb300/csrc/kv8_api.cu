@@ -27,7 +27,7 @@ kvc_status check_cache(const kvc_kv8_params *p, const kvc_kv8_cache *x, Kv8 *c) 
   if (!x->k_codes || !x->v_codes || !x->k_scale || !x->v_scale || !x->k_tail || !x->v_tail || !x->n_valid)
     return KVC_ERR_NULL;
   if (!al(x->k_codes, 16) || !al(x->v_codes, 16) || !al(x->k_tail, 16) || !al(x->v_tail, 16) ||
-      !al(x->k_scale, 16) || !al(x->v_scale, 16) || !al(x->n_valid, 4) || !al(x->pos, 4) ||
+      !al(x->k_scale, 4) || !al(x->v_scale, 4) || !al(x->n_valid, 4) || !al(x->pos, 4) ||
       !al(x->k_last, 16) || !al(x->v_last, 16) || !al(x->blocks, 8))
     return KVC_ERR_ALIGN;
   if (!x->k_last != !x->blocks || !x->v_last != !x->blocks) return KVC_ERR_NULL;  // all or none

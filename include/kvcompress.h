@@ -407,8 +407,8 @@ typedef struct {
  *
  * A call's other arguments may not overlap the cache's buffers, and its outputs nothing else
  * but where said. */
-typedef struct {       /* all dev pointers, owned by the caller; codes, scales and tails
-                          16-byte aligned */
+typedef struct {       /* all dev pointers, owned by the caller; codes and tails 16-byte
+                          aligned */
   void *k_codes;       /* e4m3 [U, cap, D] */
   void *v_codes;       /* e4m3 [U, cap, D] */
   float *k_scale;      /* fp32 [U, cap / 64] */
