@@ -335,26 +335,30 @@ __device__ __forceinline__ uint2 bf4(float4 o, float inv) {
   return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
-// The CTA's i-th unit u has n rows, whose open ones are not where a tail's rows are: marked if they
-// are in kl and vl, reported if they are gone.  Out of line: a row count is rarely lowered.  (Another
-// CTA that has planned may already have written to the unit's tail; only the CTA that has the tail
-// goes by the mark.)
+// Looks at the CTA's marked units, by all warps: the mark stays with those whose open rows are in kl and
+// vl; rows that are gone are reported.  (Another CTA that has planned may already have written to a
+// unit's tail; only the CTA that has the tail goes by the mark.)
 template <int D>
-__device__ __noinline__ int reopened(const Kv8 &c, int u, int n, int open, uint32_t *status, int *marks, int i) {
+__device__ __noinline__ void check_marks(const P8 &p, int *marks, const int *sn, int u_first, int nu, int warp, int lane) {
   constexpr int RV = D / 8;
-  bool left = true;  // the tail's first row is the one that the last call left
 #pragma unroll 1
-  for (int i = 0; i < 2 * RV; ++i) {
-    const uint4 *tl = reinterpret_cast<const uint4 *>(i < RV ? c.kt : c.vt) + (size_t)u * KB8 * RV;
-    const uint4 *ls = reinterpret_cast<const uint4 *>(i < RV ? c.kl : c.vl) + ((size_t)u * KL8 + KB8) * RV;
-    left &= same16(__ldcg(tl + i % RV), __ldcg(ls + i % RV));
+  for (int i = warp; i < nu; i += NWARP) {
+    const int u = u_first + i, n = i < SNAP ? sn[i] : ~p.snap[u];
+    if (i < SNAP ? ((marks[1 + i / 32] >> (i % 32)) & 1) == 0 : n < 0) continue;
+    const int open = open_rows(n, p.c.blocks[u]);
+    bool left = true;  // the tail's first row is the one that the last call left
+    if (lane < 2 * RV) {
+      const uint4 *tl = reinterpret_cast<const uint4 *>(lane < RV ? p.c.kt : p.c.vt) + (size_t)u * KB8 * RV;
+      const uint4 *ls = reinterpret_cast<const uint4 *>(lane < RV ? p.c.kl : p.c.vl) + ((size_t)u * KL8 + KB8) * RV;
+      left = same16(__ldcg(tl + lane % RV), __ldcg(ls + lane % RV));
+    }
+    left = __all_sync(0xffffffffu, left);
+    if (lane == 0 && !(left && open == OPEN_LAST)) {
+      if (left && open == OPEN_GONE) set_status(p.status, KVC_DEV_BAD_STATE);
+      if (i < SNAP) atomicAnd(marks + 1 + i / 32, ~(1 << (i % 32)));
+      else p.snap[u] = n;
+    }
   }
-  if (left && open == OPEN_GONE) set_status(status, KVC_DEV_BAD_STATE);
-  if (!left || open != OPEN_LAST) return n;
-  marks[0] = 1;
-  if (i >= SNAP) return ~n;
-  atomicOr(marks + 1 + i / 32, 1 << (i % 32));
-  return n;
 }
 
 // The new row is the first of a block, or joins rows that are kept: the kept ones go back to the tail,
@@ -635,11 +639,19 @@ __global__ void __launch_bounds__(NTH, 1)
       n = clamped(p.c.n_valid[u]);
       open = p.c.blocks ? open_rows(n, p.c.blocks[u]) : OPEN_TAIL;
     }
-    if (open != OPEN_TAIL) n = reopened<D>(p.c, u, n, open, p.status, const_cast<int *>(misc + M_RE), i);
+    if (open != OPEN_TAIL) {
+      misc[M_RE] = 1;
+      if (i < SNAP) atomicOr(const_cast<int *>(misc) + M_RE + 1 + i / 32, 1 << (i % 32));
+      else n = ~n;
+    }
     if (i < SNAP) sn[i] = n;
     else p.snap[u] = n;
   }
   __syncthreads();
+  if (misc[M_RE]) {  // rarely: a row count was lowered
+    check_marks<D>(p, const_cast<int *>(misc) + M_RE, sn, u_first, nu, warp, lane);
+    __syncthreads();
+  }
   // The slots at which its first unit's share begins and its last one's ends, within the unit.  (By
   // way of a shuffle, for the compiler would compute them again wherever they are used.)
   const int lo_first = uniform(C > 0 ? (b - p_first) * C : max(s0 - p_first, 0));
@@ -969,6 +981,14 @@ __global__ void __launch_bounds__(NTH, 1)
     if (nu > 0) write_q(0);
     if (lane == 0) mbar_arrive(bar + B_START);
     for (int k = 1; k < nu && ok; ++k) write_q(k);
+    // then blocks that begin, and kept rows that go back to the tail: not before the queries, for the
+    // softmax warps wait for those (1216 units of 544 rows, D = 64, 8 heads: 33.0 us; in write_q 41.5)
+    if (app && p.c.blocks && ok)
+#pragma unroll 1
+      for (int k = 0; k < nu; ++k) {
+        const Seg g = seg_at(k);
+        if (g.tail && g.add && (g.tail_old == 0 || kept_rows(g.u))) open_block<D>(p, g.u, g.n0, lane);
+      }
   } else if (warp < W_OUT) {
     // ------------------ softmax: two sets of four warps, alternate tiles ------------------
     const int set = (warp - W_SM) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
@@ -1294,12 +1314,6 @@ __global__ void __launch_bounds__(NTH, 1)
     // The CTA that finishes a shared unit's last segment merges them: this warp, while the
     // others stream on (a fence and a count take microseconds behind the tiles), or the whole
     // CTA at its end.  Only the first two segments of a CTA can be of shared units.
-    if (app && p.c.blocks)
-#pragma unroll 1
-      for (int k = 0; k < nu; ++k) {
-        const Seg g = seg_at(k);
-        if (g.tail && g.add && (g.tail_old == 0 || kept_rows(g.u))) open_block<D>(p, g.u, g.n0, lane);
-      }
     int si = 0;
     auto count_shared = [&](int k) {
       const Seg g = seg_at(k);

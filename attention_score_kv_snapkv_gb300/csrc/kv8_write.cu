@@ -125,6 +125,11 @@ __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8AppendArgs 
   const int t = threadIdx.x, u = blockIdx.x / (2 * per), x = blockIdx.x - u * 2 * per, j = x >> 1;
   const bool is_v = x & 1;
   wait_for_stream();
+  const int piece = t % RV, row0 = t / RV;
+  uint4 *tail = reinterpret_cast<uint4 *>(is_v ? a.c.vt : a.c.kt) + (size_t)u * KB8 * RV;
+  uint4 head = make_uint4(0, 0, 0, 0), copy = head;  // the tail's first row, and its copy
+  if (a.c.blocks && j == 0 && t < RV) head = tail[t], copy = first_row(a.c, u, is_v)[t];
+  const int2 blk = a.c.blocks ? a.c.blocks[u] : make_int2(-1, -1);
   int n0 = a.c.n_valid[u];
   int m = a.counts ? a.counts[u] : a.m;
   bool bad = false, full = false;
@@ -135,21 +140,15 @@ __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8AppendArgs 
     set_status(status, (bad ? KVC_DEV_BAD_STATE : 0u) | (full ? KVC_DEV_CACHE_FULL : 0u));
   const int n1 = n0 + m, b = n0 / KB8 + j, last = n1 / KB8;
   const uint4 *src = reinterpret_cast<const uint4 *>(is_v ? a.v : a.k) + (size_t)u * a.m * RV;
-  uint4 *tail = reinterpret_cast<uint4 *>(is_v ? a.c.vt : a.c.kt) + (size_t)u * KB8 * RV;
-  const int piece = t % RV, row0 = t / RV;
   const bool fills = b < last;
-  const int2 blk = a.c.blocks ? a.c.blocks[u] : make_int2(-1, -1);
   const int keep = n0 % KB8 ? n0 / KB8 : last - 1;        // the completed block whose rows are kept
   const bool opens = a.c.blocks && j == 0 && m > 0;       // this CTA leaves the tail's first row
-  uint4 w[NP], head = make_uint4(0, 0, 0, 0);             // head: the tail's first row
+  const int open = opens ? open_rows(n0, blk) : OPEN_TAIL;
+  uint4 w[NP];
   const uint4 *old = tail;                                // the open block's rows
-  if (opens) {
-    if (t < RV) head = tail[t];
-    const int open = open_rows(n0, blk);
-    if (open != OPEN_TAIL && __syncthreads_and(t >= RV || same16(head, first_row(a.c, u, is_v)[t]))) {
-      if (open == OPEN_LAST) old = last_rows(a.c, u, is_v);
-      else if (t == 0) set_status(status, KVC_DEV_BAD_STATE);
-    }
+  if (open != OPEN_TAIL && __syncthreads_and(same16(head, copy))) {
+    if (open == OPEN_LAST) old = last_rows(a.c, u, is_v);
+    else if (t == 0) set_status(status, KVC_DEV_BAD_STATE);
   }
   if (fills) {
 #pragma unroll
