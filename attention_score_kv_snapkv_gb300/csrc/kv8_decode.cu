@@ -9,15 +9,15 @@
 //   elements under 2^-14 of the head's largest (2^-21 of it at most is lost), into two e4m3
 //   terms, q 2^-e = hi + lo / 16 (bf16 has 8 significant bits, e4m3 holds 4, and the rounded
 //   remainder fits 4), which take a column each; the logit is (hi + lo / 16) 2^e scale_k.
-// * O^T = V^T . P^T (128 lanes x 16 or 32 columns): a weight is split the same way into three
-//   e4m3 terms (12 bits), a column each.  The weight of key j in a tile is
-//   exp2(s_j + log2 scale_v - M) with M the tile's largest s_j + log2 scale_v, so V's scale
-//   costs nothing and blocks of very different sizes lose no bits to each other.  (A block of zeros
-//   has the scale 1, which says nothing of its size: it is looked for, and counts with the least.)  A tile's
-//   product is not accumulated in tensor memory: four warps read it, one lane a thread, and add
-//   it to their registers with the running maximum's factor, so nothing in tensor memory is
-//   ever rescaled, and a weight keeps 12 bits down to 2^-14 of its own tile's largest and is
-//   off by at most 2^-26 of it below that.
+// * O^T = V^T . P^T (128 lanes x 16 or 32 columns): a weight is rounded to fp16 (11 bits: off by at
+//   most 2^-11 of itself) and split the same way into three e4m3 terms, a column each.  The weight
+//   of key j in a tile is exp2(s_j + log2 scale_v - M) with M the tile's largest s_j + log2 scale_v,
+//   so V's scale costs nothing and blocks of very different sizes lose no bits to each other.  (A
+//   block of zeros has the scale 1, which says nothing of its size: it is looked for, and counts
+//   with the least.)  A tile's product is not accumulated in tensor memory: four warps read it, one
+//   lane a thread, and add it to their registers with the running maximum's factor, so nothing in
+//   tensor memory is ever rescaled, and a weight keeps its 11 bits down to 2^-14 of its own tile's
+//   largest and is off by at most 2^-26 of it below that.
 // * D = 64 lies two keys to a 128-byte row: a tile is then 256 keys, S takes two products (the
 //   rows' first and second halves), and one O product serves both, lanes 0-63 the first keys,
 //   64-127 the second, each half of the lanes reading its half of the columns.
@@ -26,7 +26,7 @@
 // * The plan is made on the device, from the row counts, so ragged batches balance and the
 //   capacity costs nothing.  The units' blocks, and a tile's worth of slots for each tail, form
 //   one sequence that is split evenly over one CTA an SM; where the units are few, every CTA
-//   instead takes up to C slots of one unit (U = 8, 300 rows: 6.8 us against 8.0).  A CTA takes its
+//   instead takes up to C slots of one unit (U = 8, 300 rows: 8.0 us became 6.8).  A CTA takes its
 //   last unit first, so that shared units are done early.  The last CTA to finish a shared unit
 //   merges its segments: a warp of its own does while the others stream on (a fence and a count
 //   take up to 5 us behind the tiles; in the queries' warp they cost 3 us of 34 at U = 512), or
@@ -39,11 +39,11 @@
 //
 // Warps: TMA; S; PV; queries; 2 x 4 softmax (alternate tiles); 4 output; merge.  Four tiles may
 // lie between any two of them.
-// Measured (GB300, graph of calls on three caches in turn, against 6.79 TB/s of measured copy):
-// 64 units of 131050 rows, G = 1: 309 us (2.15 GB, 102%); 512 units of 1100 rows, G = 4, with
-// the append: 31 us (0.15 GB, 70%: 7 us are launch, plan, first tile and end, the rest runs at
-// 6.6 TB/s); 192 ragged units up to 8191 rows, D = 64, G = 8: 27 us (0.10 GB, 56%: short units'
-// ends and the softmax's latency); 8 units of 300 rows: 7 us (latency).
+// Measured (GB300, graph of calls with the append on three caches in turn, against 6.68 TB/s of
+// measured copy): 64 units of 131050 rows, G = 1: 311 us (2.15 GB, 103%); 512 units of 1100 rows,
+// G = 4: 31.7 us (0.15 GB, 70%: 7 us are launch, plan, first tile and end, the rest runs at 6.6
+// TB/s); 192 ragged units up to 8191 rows, D = 64, G = 8: 27.0 us (0.10 GB, 57%: short units' ends
+// and the softmax's latency); 8 units of 300 rows: 7.0 us (latency).
 #include <math.h>
 
 #include "kv8.cuh"
@@ -112,7 +112,7 @@ constexpr int M_RED = 46;      // [4] quantisation
 constexpr int M_VALID = 50;    // [2] a shared unit's segment was completed
 constexpr int M_TODO = 52;     // [2][4] this CTA merges it at the end: the Shared (nseg 0: it does not)
 static_assert(sizeof(WaitState) == 4 * (M_TMEM - M_WAIT) && B_MISC % 8 == 0, "the waits' state");
-constexpr int M_RE = 60;       // [1 + SNAP / 32] whether, and which of, the CTA's units have their open rows in kl and vl
+constexpr int M_RE = 60;       // [1 + SNAP / 32] whether, and which, units have their open rows in kl and vl
 static_assert(B_MISC + 4 * (M_RE + 1 + SNAP / 32) <= 768, "barrier area");
 
 struct P8 {
@@ -160,7 +160,7 @@ __device__ __forceinline__ uint32_t elect_one() {
 // x, of which the compiler knows nothing, so that it does not compile what follows once for each
 // value: the warps' code together is more than an SM's instruction cache holds (without this, the
 // loops that are kept rolled and the plan's results in shuffles, 1216 units of 544 rows, D = 64,
-// 8 heads take 41 us instead of 30).
+// 8 heads took 41 us, with it 30; 33 since rows can be taken back and zeros are looked for).
 __device__ __forceinline__ bool opaque(bool x) {
   uint32_t r = x;
   asm volatile("" : "+r"(r));
@@ -258,7 +258,8 @@ __device__ __forceinline__ float fin(float m) { return m == -INFINITY ? 0.f : m;
 // blk * block_bytes.  A block of zeros has the scale 1, which says nothing of its size, and would let
 // its keys set the reference of a tile whose other blocks are small: where the codes are zeros (and
 // NaNs, which come out whatever their weight is) alone, the scale becomes the least there is.  Looked at
-// only where a scale is 1, and a block that is not zeros mostly shows it in its first 16 codes.
+// only where a scale is 1, and a block that is not zeros mostly shows it in its first 16 codes: 512
+// units of 1100 rows take 31 us with or without scales of 1, 49 us when all of V is zeros.
 __device__ __forceinline__ bool zero_codes(const uint4 *at) {
   const uint4 x = __ldcg(at);
   // a magnitude m that is neither 0 nor 127 leaves a bit of m + 1 between the lowest and the highest
@@ -339,7 +340,8 @@ __device__ __forceinline__ uint2 bf4(float4 o, float inv) {
 // vl; rows that are gone are reported.  (Another CTA that has planned may already have written to a
 // unit's tail; only the CTA that has the tail goes by the mark.)
 template <int D>
-__device__ __noinline__ void check_marks(const P8 &p, int *marks, const int *sn, int u_first, int nu, int warp, int lane) {
+__device__ __noinline__ void check_marks(const P8 &p, int *marks, const int *sn, int u_first, int nu, int warp,
+                                         int lane) {
   constexpr int RV = D / 8;
 #pragma unroll 1
   for (int i = warp; i < nu; i += NWARP) {
@@ -1102,7 +1104,7 @@ __global__ void __launch_bounds__(NTH, 1)
         if (!tail) {
 #pragma unroll
           for (int jj = 0; jj < KPR; ++jj) {
-            // three e4m3 terms, a factor 16 apart, of each weight rounded to fp16 (2^-12; the
+            // three e4m3 terms, a factor 16 apart, of each weight rounded to fp16 (2^-11; the
             // differences are exact there)
             uint32_t t[3][HB / 4];
             const __half2 x16 = __float2half2_rn(16.f);

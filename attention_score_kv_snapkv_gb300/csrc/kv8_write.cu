@@ -14,7 +14,7 @@ namespace kvc {
 namespace {
 
 // The write and the append may be launched while the kernel before them in the stream still runs,
-// and wait for it (an append of 700 rows 9.6 us against 10.3).  They let the next one be launched
+// and wait for it (an append of 700 rows 8.7 us against 9.4).  They let the next one be launched
 // only by ending: an early trigger made a selection every time 38.7 us instead of 34.7; and the
 // read-back, one short wave, took 3.8 us so and 2.8 launched plainly.  Their sources may have been
 // written by the kernel that they overlap, so they are not loaded by way of the read-only cache, whose
@@ -46,10 +46,11 @@ __device__ __forceinline__ uint4 *first_row(const Kv8 &c, int u, bool is_v) {
 // rows are 64 wide (half as much each: as many bytes in flight, half as many CTAs).  Loads are
 // without branches, so that all of a thread's are in flight at once.
 // Measured (GB300, graph of calls on three sources in turn): 128 units of 16384 rows, D = 128,
-// 227 us (1.61 GB, 7.1 TB/s: 105% of the measured copy), D = 64 116 us; 192 ragged units of up to
-// 1023 rows, D = 64, 7.3 us (77%).  One load behind each branch took 285 us for the first (a
-// persistent CTA an SM with a ring of bulk copies 261) and 153 and 9.7 us for the others.
-// 10 CTAs an SM: with 12 some registers spill (230 us), with 8 ragged batches take 5% longer.
+// 225 us (1.61 GB, 7.2 TB/s: 107% of the measured copy), D = 64 115 us; 192 ragged units of up to
+// 1023 rows, D = 64, 8.1 us (71%).  One load behind each branch took 285 us for the first (a
+// persistent CTA an SM with a ring of bulk copies 261) and 153 us for the second.
+// 10 CTAs an SM (48 registers, no spills): with 12 (40 registers) 52 to 104 bytes spill, 229 and 117
+// us; with 8 a selection of 1024 of 16384 rows takes 36.4 us, with 10 34.5.
 template <int D>
 __global__ void __launch_bounds__(KV8_NT, 10) kv8_write_kernel(const Kv8WriteArgs a, uint32_t *status) {
   constexpr int RV = D / 8, NP = KB8 * RV / KV8_NT, RS = KV8_NT / RV;  // RS rows a step
@@ -117,7 +118,8 @@ __global__ void __launch_bounds__(KV8_NT, 10) kv8_write_kernel(const Kv8WriteArg
 // and CTA 0, whose block starts with the tail's rows, then writes the new tail.  The row count
 // changes when every CTA of the unit has read it: the last one to count itself writes it.
 // The rows of one completed block are kept as they came, so that the row count may be lowered into
-// it: the block that held rows before, else the last one (64 units of 700 rows: 64 KB more to 358).
+// it: the block that held rows before, else the last one (64 units of 700 rows: 32 KB
+// a unit more to 537; 8.7 us, before that and the first row's copy 7.3).
 template <int D>
 __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8AppendArgs a, int per, uint32_t *status) {
   constexpr int RV = D / 8, NP = KB8 * RV / KV8_NT, RS = KV8_NT / RV;

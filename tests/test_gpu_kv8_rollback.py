@@ -300,3 +300,26 @@ def test_refusals(kvc):
                 {"blocks": c.blocks[..., :1].contiguous()}, {"blocks": c.blocks.long()}, {"blocks": c.blocks.cpu()}):
         with pytest.raises((TypeError, ValueError)):
             kvc.KV8Cache.from_tensors(**t, **{**more, **bad})
+
+
+def test_a_hundred_thousand_units_taken_back(kvc):
+    """More units to a CTA than it keeps row counts for; a third are lowered into the block that the
+    append completed, the others within the open one, or not at all."""
+    U, D, cap, n0, m = (10, 100, 100), 64, 128, 60, 9
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows = [torch.randn(U + (n0 + m, D), generator=g, device="cuda").to(BF) for _ in "kv"]
+    cut = lambda a, b: [x[..., a:b, :].contiguous() for x in rows]  # noqa: E731
+    cache = kvc.kv8_append(*cut(n0, n0 + m), kvc.kv8_write(*cut(0, n0), kvc.KV8Cache(*U, D, cap)))
+    n = n0 + torch.randint(0, 12, U, generator=g, device="cuda", dtype=torch.int32).clamp(max=m)
+    q = torch.randn(U[:2] + (U[2], D), generator=g, device="cuda").to(BF)
+    kn, vn = (torch.randn(U + (D,), generator=g, device="cuda").to(BF) for _ in "kv")
+    cache.n_valid.copy_(n)
+    want = kvc.kv8_write(*rows, kvc.KV8Cache(*U, D, cap), lengths=n)
+    for step in range(2):
+        assert torch.equal(bits(kvc.kv8_decode_attn(q, cache)), bits(kvc.kv8_decode_attn(q, want)))
+        for x, y in zip(kvc.kv8_read(cache), kvc.kv8_read(want)):
+            assert torch.equal(bits(x), bits(y))
+        if step == 0:
+            a, b = (kvc.kv8_decode_attn(q, c, k_new=kn, v_new=vn, new_pos=5) for c in (cache, want))
+            assert torch.equal(bits(a), bits(b))
+    assert torch.equal(cache.n_valid, want.n_valid) and kvc.kvc_device_status() == 0
