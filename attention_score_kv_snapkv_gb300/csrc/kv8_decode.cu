@@ -40,10 +40,10 @@
 // Warps: TMA; S; PV; queries; 2 x 4 softmax (alternate tiles); 4 output; merge.  Four tiles may
 // lie between any two of them.
 // Measured (GB300, graph of calls with the append on three caches in turn, against 6.68 TB/s of
-// measured copy): 64 units of 131050 rows, G = 1: 311 us (2.15 GB, 103%); 512 units of 1100 rows,
-// G = 4: 31.7 us (0.15 GB, 70%: 7 us are launch, plan, first tile and end, the rest runs at 6.6
-// TB/s); 192 ragged units up to 8191 rows, D = 64, G = 8: 27.0 us (0.10 GB, 57%: short units' ends
-// and the softmax's latency); 8 units of 300 rows: 7.0 us (latency).
+// measured copy): 64 units of 131050 rows, G = 1: 310 us (2.15 GB, 104%); 512 units of 1100 rows,
+// G = 4: 31.3 us (0.15 GB, 70%: 7 us are launch, plan, first tile and end, the rest runs at 6.6
+// TB/s); 192 ragged units up to 8191 rows, D = 64, G = 8: 27.5 us (0.10 GB, 56%: short units' ends
+// and the softmax's latency); 8 units of 300 rows: 7.2 us (latency).
 #include <math.h>
 
 #include "kv8.cuh"

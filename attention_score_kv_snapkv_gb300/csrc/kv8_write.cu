@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(KV8_NT, 10) kv8_write_kernel(const Kv8WriteArg
 // changes when every CTA of the unit has read it: the last one to count itself writes it.
 // The rows of one completed block are kept as they came, so that the row count may be lowered into
 // it: the block that held rows before, else the last one (64 units of 700 rows: 32 KB
-// a unit more to 537; 8.7 us, before that and the first row's copy 7.3).
+// a unit more to 537; 8.9 us, without them and the first row's copy 7.3).
 template <int D>
 __global__ void __launch_bounds__(KV8_NT) kv8_append_kernel(const Kv8AppendArgs a, int per, uint32_t *status) {
   constexpr int RV = D / 8, NP = KB8 * RV / KV8_NT, RS = KV8_NT / RV;
