@@ -323,3 +323,37 @@ def test_a_hundred_thousand_units_taken_back(kvc):
             a, b = (kvc.kv8_decode_attn(q, c, k_new=kn, v_new=vn, new_pos=5) for c in (cache, want))
             assert torch.equal(bits(a), bits(b))
     assert torch.equal(cache.n_valid, want.n_valid) and kvc.kvc_device_status() == 0
+
+
+@pytest.mark.parametrize("by", ["append", "step"])
+@pytest.mark.parametrize("D,cap", [(64, 64), (128, 256)])
+def test_a_full_cache_taken_back(kvc, by, D, cap):
+    """Filled to its capacity and past it, taken back by up to a block less one row, filled again; units
+    that add nothing (counts of zero) stay as they were taken back."""
+    shape, G = (1, 3, 7), 2
+    k, v = rnd(shape + (cap - 5, D), 1), rnd(shape + (cap - 5, D), 2)
+    a, b = rnd(shape + (9, D), 3, boost=False), rnd(shape + (9, D), 4, boost=False)
+    q = rnd((1, 3, 7 * G, D), 5, boost=False).cuda()
+
+    def add(x, y, c, m):
+        if by == "append":
+            kvc.kv8_append(*dev(x, y), c, counts=m.cuda())
+        else:
+            for t in range(x.shape[3]):
+                kvc.kv8_decode_attn(q, c, k_new=x[..., t, :].contiguous().cuda(), v_new=y[..., t, :].contiguous().cuda())
+
+    cache = kvc.kv8_write(*dev(k, v), poison(kvc.KV8Cache(*shape, D, cap)))
+    full, five, nine = (torch.full(shape, n, dtype=torch.int32) for n in (cap - 5, 5, 9))
+    add(a, b, cache, nine)
+    assert kvc.kvc_device_status() == kvc.DEV_CACHE_FULL
+    check_held(kvc, cache, [(k, full), (a, five)], [(v, full), (b, five)], q)
+    back = torch.arange(21, dtype=torch.int32).view(shape) * 3                 # 0 .. 60 rows taken back
+    cache.n_valid.copy_(cap - back)
+    rows = [torch.cat([x, y[..., :5, :]], 3) for x, y in ((k, a), (v, b))]
+    kept = cap - back
+    check_held(kvc, cache, [(rows[0], kept)], [(rows[1], kept)], q)
+    m = torch.where(torch.arange(21).view(shape) % 4 == 1, 0, 3).to(torch.int32) if by == "append" else torch.full(shape, 3, dtype=torch.int32)
+    add(a[..., 6:9, :].contiguous(), b[..., 6:9, :].contiguous(), cache, m)
+    took = torch.minimum(m, back)
+    check_held(kvc, cache, [(rows[0], kept), (a[..., 6:9, :], took)], [(rows[1], kept), (b[..., 6:9, :], took)], q)
+    assert kvc.kvc_device_status() == (kvc.DEV_CACHE_FULL if (took < m).any() else 0)
